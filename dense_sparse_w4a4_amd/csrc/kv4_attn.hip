@@ -99,6 +99,13 @@ struct Tile {
   bool ok;
 };
 
+// A token's (scale, zero point) word as it is computed with: a zero point that is
+// not finite becomes a scale of NaN and a zero point of 0.  The scale reaches only
+// the rows that see the token (an unseen token's score is replaced, and its weight
+// of 0 takes the value scale by mul_zero), but zero points are a matrix operand,
+// where 0 * NaN would reach every row of the step.
+__device__ __forceinline__ uint32_t finite_zero(uint32_t w) { return (w & 0x7C000000u) == 0x7C000000u ? 0x7E00u : w; }
+
 // ONCE: the words are read by this wave alone and pass the caches by.
 template <bool ONCE, typename T>
 __device__ __forceinline__ T load_words(const uint8_t* p) {
@@ -288,7 +295,7 @@ struct FromRegisters {
 
   __device__ __forceinline__ FromRegisters(const Tile<D>& tile, uint32_t* words, int lane, uint32_t m)
       : t(tile), r(lane & 15), ch(lane >> 4), magic(m) {
-    words[lane] = t.sz;
+    words[lane] = finite_zero(t.sz);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 x = *reinterpret_cast<const uint4*>(words + 16 * h + 4 * ch);
@@ -745,7 +752,7 @@ struct StepLds {
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) v[x][lane] = o[x];
     const int i = lane & 31;
-    const uint32_t w = t0 + i < len ? t.sz : 0u;
+    const uint32_t w = t0 + i < len ? finite_zero(t.sz) : 0u;
     const float sc = half_lo(w);
     if (lane < 32) {
       kw[i] = w;

@@ -1,0 +1,122 @@
+"""Attention over the 4-bit cache where masks, scales and zero points go to
+their limits: what a row does not see has no effect on it, whatever its bits.
+
+Bounds, beside test_kv4_gpu.py's: a value is s (u - 8) + s (z + 8), two fp32
+sums that may cancel.  Each addition (one per 32 tokens, and as many again where
+waves and parts are joined) may be off by 2^-24 of a partial sum, at most 8 + Z
+times S = sum p s / sum p for zero points with |z + 8| <= Z, so 2^-23 (8 + Z) S
+for both.  A weight below fp16's normal numbers is off by 2^-25 where the largest
+is at least 2^3, 2^-28 of it: under 2^-19 of A for these contexts."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from dense_sparse_w4a4_amd import ops
+from test_kv4_gpu import _batch, _device
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ops.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def _held(cache, table, n):
+    """Word indexes (page, offset) of a sequence's first n tokens."""
+    t = np.arange(n)
+    page = cache["kq"].shape[2]
+    return table[t // page], t % page
+
+
+def _expect(cache, table, lens, news, q, causal, window, scale):
+    """fp64 (o, lse, bound of o, bound of lse) over the whole batch."""
+    parts, at = [], 0
+    q64 = q.double().numpy()
+    D = q.shape[2]
+    for i, (n, m) in enumerate(zip(lens, news)):
+        k, v = oracle.kv4_read(cache, table[i], n)
+        p, off = _held(cache, table[i], n)
+        ks, vs = cache["ksz"][p, :, off].astype(np.float64), cache["vsz"][p, :, off].astype(np.float64)
+        qq = q64[at:at + m]
+        ref = lambda x: oracle.attention_reference(qq, k, x, causal, window, scale)  # noqa: E731
+        o, lse = ref(v)
+        A, _ = ref(np.abs(v))
+        S, _ = ref(np.repeat(vs[..., :1], D, -1))
+        Z = np.abs(vs[..., 1] + 8).max(initial=0)
+        d = 2.0 ** -18 * abs(scale) * 15 * ks[..., 0].max(initial=0) * np.abs(qq).sum(-1)
+        sums = 2.0 ** -23 * (8 + Z) * S * 2 * (n / 32 + 1)
+        parts.append((o, lse, (2.0 ** -11 + 2 * d[..., None] + 2.0 ** -16 + 2.0 ** -19) * A + sums, d))
+        at += m
+    o, lse, tol, d = (np.concatenate(x) for x in zip(*parts))
+    out = 2.0 ** -11 if q.dtype == torch.float16 else 2.0 ** -8
+    with np.errstate(invalid="ignore"):
+        return o, lse, out * np.abs(o) + tol + 2.0 ** -24, d + 2.0 ** -20 * np.abs(lse) + 2.0 ** -16
+
+
+def _run(cache, table, lens, news, q, causal=True, window=0, scale=None, max_q=None):
+    lse = torch.full(q.shape[:2], 5.0, dtype=torch.float32, device="cuda")
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32).cuda()
+    out = ops.kv4_attention(q.cuda(), _device(cache), torch.from_numpy(table).cuda(),
+                            torch.tensor(lens, dtype=torch.int32).cuda(), starts, max_q=max_q, causal=causal,
+                            window=window, scale=scale, lse=lse)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def _close(got, want, rows=slice(None)):
+    (o, lse), (ro, rl, tol, ltol) = got, want
+    err = np.abs(o[rows] - ro[rows])
+    assert np.all(err <= tol[rows]), f"o: worst err/tol {np.nanmax(err / tol[rows]):.3f}, nan {np.isnan(err).sum()}"
+    empty = np.isinf(rl[rows])
+    assert np.array_equal(lse[rows][empty], rl[rows][empty])
+    assert np.all(np.abs(lse[rows] - rl[rows])[~empty] <= ltol[rows][~empty])
+
+
+def _copy(cache):
+    return {n: x.copy() for n, x in cache.items()}
+
+
+BATCH = ([300, 65, 129, 40], [37, 20, 5, 40])
+ODD = [np.nan, np.inf, -np.inf, 65504, -65504]
+
+
+@pytest.mark.parametrize("hq,hk,D,dtype", [(8, 2, 128, torch.float16), (8, 1, 64, torch.bfloat16)])
+def test_zero_points_of_tokens_that_no_row_sees(hq, hk, D, dtype):
+    """Tokens below every row's window hold any zero point, in the steps that
+    are read for the tokens beside them."""
+    lens, news = BATCH
+    cache, table, q = _batch(lens, news, hq, hk, D, 32, dtype, seed=20)
+    want = _expect(cache, table, lens, news, q, True, 21, D ** -0.5)
+    rng = np.random.default_rng(20)
+    bad = _copy(cache)
+    for i, (n, m) in enumerate(zip(lens, news)):
+        p, off = _held(cache, table[i], max(0, n - m - 20))
+        for name in ("ksz", "vsz"):
+            bad[name][p, :, off, 1] = rng.choice(ODD, (len(p), hk))
+    for max_q in (1, 40):
+        print(f"hq={hq} D={D} max_q={max_q}", flush=True)
+        _close(_run(bad, table, lens, news, q, window=21, max_q=max_q), want)
+
+
+@pytest.mark.parametrize("name", ["ksz", "vsz"])
+@pytest.mark.parametrize("odd", [np.nan, np.inf, -np.inf])
+def test_zero_points_reach_only_the_rows_that_see_them(name, odd):
+    """Row i of a sequence of 90 with 30 queries sits at 60 + i and sees the last
+    25 tokens: token 70's zero point is in rows 10 .. 29, token 47's in rows 0 .. 11."""
+    lens, news = [90], [30]
+    cache, table, q = _batch(lens, news, 4, 2, 128, 32, torch.float16, seed=21)
+    want = _expect(cache, table, lens, news, q, True, 25, 128 ** -0.5)
+    for t, sees in ((70, np.arange(10, 30)), (47, np.arange(0, 12))):
+        bad = _copy(cache)
+        p, off = _held(cache, table[0], 90)
+        bad[name][p[t], :, off[t], 1] = odd
+        others = np.setdiff1d(np.arange(30), sees)
+        for max_q in (1, 30):
+            got = _run(bad, table, lens, news, q, window=25, max_q=max_q)
+            assert not np.isfinite(got[0][sees]).any()
+            _close(got, want, others)
