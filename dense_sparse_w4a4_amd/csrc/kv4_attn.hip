@@ -17,7 +17,8 @@
 // of two large sums (measured 3x the error of fp32 softmax at 131075 tokens),
 // so they are centred: OR-ed under the exponent of 1024 the code is 1024 + u
 // (or 1024 + 16u), and one packed operation on two codes makes it u - 8,
-// exactly; the zero points' sum takes z + 8.
+// exactly; the zero points' sum takes z + 8, as two fp16 whole numbers (its nearest
+// and the rest, 0 for |z| <= 2040) in different rows of one product.
 //
 // Operand layout.  Scores are computed transposed, S^T = K Q^T (A: 16 tokens,
 // B: 16 query columns), so that lane (r = lane % 16, c = lane / 16) receives
@@ -105,6 +106,20 @@ struct Tile {
 // of 0 takes the value scale by mul_zero), but zero points are a matrix operand,
 // where 0 * NaN would reach every row of the step.
 __device__ __forceinline__ uint32_t finite_zero(uint32_t w) { return (w & 0x7C000000u) == 0x7C000000u ? 0x7E00u : w; }
+
+// z + 8 as its nearest fp16 and the rest, exactly, for whole z: where |z| < 8 the
+// sum is exact, above it the larger addend gives the sum's error back.
+struct ZeroPair {
+  _Float16 near, rest;
+};
+__device__ __forceinline__ ZeroPair zero_pair(uint32_t word) {
+  const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(word >> 16));
+  const _Float16 near = z + 8.0f16;
+  return {near, 8.0f16 - (near - z)};
+}
+__device__ __forceinline__ uint32_t with_zero(uint32_t word, _Float16 z) {
+  return (word & 0xFFFFu) | ((uint32_t)__builtin_bit_cast(uint16_t, z) << 16);
+}
 
 // ONCE: the words are read by this wave alone and pass the caches by.
 template <bool ONCE, typename T>
@@ -198,7 +213,7 @@ struct Columns {
   uint4 q[NC][D / 32];
   float qsum[NC], mul[NC];      // sum of the scaled queries; scores' factor to exponents of two
   int hi[NC], lo[NC];           // the column sees tokens lo <= t < hi
-  v4f o[NC][D / 16], z[NC];
+  v4f o[NC][D / 16], z[NC];     // z: rows 0, 4, 8, 12 of the product sum the near parts, the others the rests
   float m[NC], top[NC], l[NC];  // top: the score that raises m
   float cs;                     // power of two on w = p * s_v
   float limit;                  // the largest s_v that cs allows
@@ -216,6 +231,7 @@ struct Columns {
     cs = 1.0f;
     limit = 0.0f;
   }
+  __device__ __forceinline__ float zeros(int n) const { return z[n][0] + z[n][1]; }
   __device__ __forceinline__ void rescale(int n, float f) {
     z[n] *= f;
 #pragma unroll
@@ -284,7 +300,9 @@ __device__ __forceinline__ void value_operands(const Tile<D>& t, int r, uint32_t
 // What a step takes of its 32 tokens: operands, and for the lane's own tokens
 // (16h + 4c + i) the words with the keys' zero points, the scales, the zero
 // points' operand and the largest value scale.  Here from the wave's own
-// registers, the words through 256 bytes of LDS of its own.
+// registers, the words through 512 bytes of LDS of its own: the keys' words, the
+// values' with the near part of z + 8 and once more with the rest, for the rows
+// (lanes) that take the one or the other.
 template <int D>
 struct FromRegisters {
   const Tile<D>& t;
@@ -295,11 +313,15 @@ struct FromRegisters {
 
   __device__ __forceinline__ FromRegisters(const Tile<D>& tile, uint32_t* words, int lane, uint32_t m)
       : t(tile), r(lane & 15), ch(lane >> 4), magic(m) {
-    words[lane] = finite_zero(t.sz);
+    const uint32_t word = finite_zero(t.sz);
+    const ZeroPair z = zero_pair(word);
+    words[lane] = lane < 32 ? word : with_zero(word, z.near);
+    words[lane ^ 96] = with_zero(word, z.rest);  // 64 .. 95; the keys' lanes' are not used
+    const uint32_t* const values = words + (r & 3 ? 64 : 32);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 x = *reinterpret_cast<const uint4*>(words + 16 * h + 4 * ch);
-      const uint4 y = *reinterpret_cast<const uint4*>(words + 32 + 16 * h + 4 * ch);
+      const uint4 y = *reinterpret_cast<const uint4*>(values + 16 * h + 4 * ch);
       kw[4 * h] = x.x; kw[4 * h + 1] = x.y; kw[4 * h + 2] = x.z; kw[4 * h + 3] = x.w;
       vw[4 * h] = y.x; vw[4 * h + 1] = y.y; vw[4 * h + 2] = y.z; vw[4 * h + 3] = y.w;
     }
@@ -322,10 +344,7 @@ struct FromRegisters {
   __device__ __forceinline__ uint4 zeros() const {
     uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v2half zz = __builtin_bit_cast(v2half, __builtin_amdgcn_perm(vw[2 * i + 1], vw[2 * i], 0x07060302u));
-      p[i] = __builtin_bit_cast(uint32_t, zz + v2half{8.0f16, 8.0f16});
-    }
+    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_perm(vw[2 * i + 1], vw[2 * i], 0x07060302u);
     return make_uint4(p[0], p[1], p[2], p[3]);
   }
   __device__ __forceinline__ void prepare_values() { value_operands<D>(t, r, magic, v); }
@@ -414,7 +433,7 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
     w[n] = make_uint4(pack2<kF16>(y[0], y[1]), pack2<kF16>(y[2], y[3]), pack2<kF16>(y[4], y[5]), pack2<kF16>(y[6], y[7]));
   }
 
-  // the zero points' sum, in every row of its product, and the values
+  // the zero points' sums and the values
   const uint4 z = t.zeros();
 #pragma unroll
   for (int n = 0; n < NC; ++n) s.z[n] = mfma16(z, w[n], s.z[n]);
@@ -541,7 +560,7 @@ template <int DT, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv4_decode_kernel(Kv4AttnArgs a) {
   __shared__ __align__(16) float red[kWaves][16][D + 4];
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
-  __shared__ __align__(16) uint32_t words[kWaves][64];
+  __shared__ __align__(16) uint32_t words[kWaves][128];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = threadIdx.x & 63;
   const int r = lane & 15, ch = lane >> 4;
@@ -611,7 +630,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_decode_kernel(Kv4AttnArgs 
     });
 
     // join the waves: everything at the largest maximum, in true units
-    const float l = column_sum(s.l[0]), z = s.z[0][0], me = s.m[0] * s.mul[0];
+    const float l = column_sum(s.l[0]), z = s.zeros(0), me = s.m[0] * s.mul[0];
     if (ch == 0) red_m[wave][r] = me;
     __syncthreads();
     const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
@@ -737,7 +756,7 @@ struct StepLds {
   uint4 k[D / 16][64], v[D / 16][64];  // [operand][lane]
   uint32_t kw[32];
   float ks[32], vs[32];
-  uint16_t z[32];  // zero point + 8
+  _Float16 near[32], rest[32];  // of zero point + 8
   float top;
   int ok;
 
@@ -759,7 +778,9 @@ struct StepLds {
       ks[i] = sc;
     } else {
       vs[i] = sc;
-      z[i] = f2h_bits(half_hi(w) + 8.0f);
+      const ZeroPair z = zero_pair(w);
+      near[i] = z.near;
+      rest[i] = z.rest;
     }
     float m = sc < 65504.0f ? sc : (sc == sc ? 65504.0f : 0.0f);  // NaN does not count
     m = fmaxf(m, __shfl_xor(m, 1));
@@ -796,7 +817,8 @@ struct FromLds {
   __device__ __forceinline__ float value_scale(int i) const { return vs[i]; }
   __device__ __forceinline__ float largest() const { return t.top; }
   __device__ __forceinline__ uint4 zeros() const {
-    const uint2 a = *reinterpret_cast<const uint2*>(t.z + 4 * ch), b = *reinterpret_cast<const uint2*>(t.z + 16 + 4 * ch);
+    const _Float16* const z = (lane & 3 ? t.rest : t.near) + 4 * ch;
+    const uint2 a = *reinterpret_cast<const uint2*>(z), b = *reinterpret_cast<const uint2*>(z + 16);
     return make_uint4(a.x, a.y, b.x, b.y);
   }
   __device__ __forceinline__ void prepare_values() {}
@@ -896,12 +918,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_tile_kernel(Kv4AttnArgs a)
   for (int n = 0; n < NC; ++n) {
     const float l = column_sum(s.l[n]), me = s.m[n] * s.mul[n];
     if (row[n] < 0) continue;
+    const float z = s.zeros(n);
     const float f = parts == 1 ? (l == 0.0f ? 0.0f : unit / l) : unit;  // no visible token: 0
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float v[D / 16];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) v[x] = (s.o[n][x][i] + s.z[n][0]) * f;
+      for (int x = 0; x < D / 16; ++x) v[x] = (s.o[n][x][i] + z) * f;
       const int d = ch * (D / 4) + i * (D / 16);
       if (parts == 1) {
         uint16_t* const to = a.out + row[n] * a.ldo + (int64_t)hq[n] * D + d;

@@ -120,3 +120,20 @@ def test_zero_points_reach_only_the_rows_that_see_them(name, odd):
             got = _run(bad, table, lens, news, q, window=25, max_q=max_q)
             assert not np.isfinite(got[0][sees]).any()
             _close(got, want, others)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_zero_points_are_exact_whole_numbers(D, max_q):
+    """One visible token: its weight is 1, and the output is the held value s (u
+    + z) rounded once (the sum p may be off by fp32's rounding), for zero points up to the largest of fp16."""
+    zeros = [2040, 2041, 2043, 2045, 2047, 2048, 2050, 4092, 16368, 16400, 65504]
+    zeros = np.array([-z for z in zeros] + [0, -7, -8] + zeros, np.float64)
+    n = len(zeros)
+    cache, table, q = _batch([1] * n, [1] * n, 4, 2, D, 32, torch.float16, seed=22)
+    cache["vsz"][table[:, 0], :, 0] = np.stack([np.full(n, 0.5), zeros], -1)[:, None, :]
+    exact = np.stack([oracle.kv4_read(cache, table[i], 1)[1][0] for i in range(n)]).repeat(2, 1)  # [n, 4, D]
+    got, _ = _run(cache, table, [1] * n, [1] * n, q, max_q=max_q)
+    half = 0.5 * np.spacing(np.abs(exact).astype(np.float16)).astype(np.float64)
+    err = np.abs(got - exact)
+    assert np.all(err <= half * (1 + 2.0 ** -8)), (err / half).max(axis=(1, 2))
