@@ -33,8 +33,10 @@
 // exchange.  The weights w = p * s_v are rounded to fp16 for the matrix core
 // (to nearest); the zero points' sum (of w (z_v + 8)) is one more product with
 // the same rounded w, so that rounding scales v and not its offset.  w is kept
-// in fp16's normal range by a power of two that follows the largest s_v seen.
-// l sums the unrounded p.
+// in fp16's normal range by a power of two of the column's own, which follows the
+// largest w that the column has seen: not the largest s_v, since a token that the
+// column does not see, or whose weight is next to nothing, would push the weights
+// that count into fp16's subnormals.  l sums the unrounded p.
 #include <algorithm>
 
 #include "kv4.h"
@@ -59,6 +61,7 @@ typedef const __attribute__((address_space(4))) int32_t* cint_p;
 constexpr int kWaves = 4;            // waves of a workgroup
 constexpr int kStep = kWaves * kKv4Tile;  // tokens of one step of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kMostCs = 0x1p100f;  // of a column that has seen no value but 0
 constexpr float kLow = -1e10f;  // below every finite score s_k (q.u + z sum q) of scaled queries, all under 1e8
 
 __device__ __forceinline__ float xor16(float v, bool take_max) {
@@ -76,6 +79,14 @@ __device__ __forceinline__ float xor32(float v, bool take_max) {
 // Over the four lanes r, r + 16, r + 32, r + 48.
 __device__ __forceinline__ float column_max(float v) { return xor32(xor16(v, true), true); }
 __device__ __forceinline__ float column_sum(float v) { return xor32(xor16(v, false), false); }
+
+// Not shared with the same expression elsewhere: what a rare branch computes
+// again stays inside it.
+template <typename T>
+__device__ __forceinline__ T opaque(T v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
@@ -215,8 +226,7 @@ struct Columns {
   int hi[NC], lo[NC];           // the column sees tokens lo <= t < hi
   v4f o[NC][D / 16], z[NC];     // z: rows 0, 4, 8, 12 of the product sum the near parts, the others the rests
   float m[NC], top[NC], l[NC];  // top: the score that raises m
-  float cs;                     // power of two on w = p * s_v
-  float limit;                  // the largest s_v that cs allows
+  float cs[NC], big[NC];        // power of two on w = p * s_v; the largest w that was looked for
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -227,9 +237,9 @@ struct Columns {
       z[n] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i] = v4f{0.f, 0.f, 0.f, 0.f};
+      cs[n] = kMostCs;
+      big[n] = 0.0f;
     }
-    cs = 1.0f;
-    limit = 0.0f;
   }
   __device__ __forceinline__ float zeros(int n) const { return z[n][0] + z[n][1]; }
   __device__ __forceinline__ void rescale(int n, float f) {
@@ -326,15 +336,11 @@ struct FromRegisters {
       vw[4 * h] = y.x; vw[4 * h + 1] = y.y; vw[4 * h + 2] = y.z; vw[4 * h + 3] = y.w;
     }
   }
-  // tokens past the sequence's end: no value scale
-  __device__ __forceinline__ void hide(int t0, int len) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) vw[i] = t0 + 16 * (i >> 2) + 4 * ch + (i & 3) < len ? vw[i] : 0u;
-  }
   __device__ __forceinline__ uint4 key(int h, int j) const { return codes8(t.k[h][j]); }
   __device__ __forceinline__ uint32_t key_word(int i) const { return kw[i]; }
   __device__ __forceinline__ float key_scale(int i) const { return half_lo(kw[i]); }
   __device__ __forceinline__ float value_scale(int i) const { return half_lo(vw[i]); }
+  __device__ __forceinline__ float value_scale_again(int i) const { return half_lo(opaque(vw[i])); }
   __device__ __forceinline__ float largest() const {
     v2half m = __builtin_bit_cast(v2half, vw[0]);
 #pragma unroll
@@ -352,9 +358,9 @@ struct FromRegisters {
 };
 
 // One 32-token step from token t0.  edge (uniform): some column may not see
-// some token of it; tokens from `len` on were never written.
+// some token of it.
 template <int D, int NC, typename F>
-__device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0, int len, int ch) {
+__device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0, int ch) {
   // scores
   v4f a[NC][2];
 #pragma unroll
@@ -374,7 +380,6 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
     for (int n = 0; n < NC; ++n) x[n][i] = fmaf(half_hi(t.key_word(i)), s.qsum[n], a[n][i >> 2][i & 3]) * sk;
   }
   if (__builtin_expect(edge, 0)) {
-    t.hide(t0, len);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int tok = t0 + 16 * (i >> 2) + 4 * ch + (i & 3);
@@ -383,28 +388,18 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
     }
   }
 
-  // rare: a score far above its column's maximum, or a value scale above what
-  // the weights' power of two allows
+  // rare: a score far above its column's maximum, or a value scale so large that
+  // a weight might leave fp16's range (w <= 2^6 * 2^9)
   const float vtop = t.largest();
-  bool raise = vtop > s.limit;
+  bool raise = false;
   float tm[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     tm[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])),
                   fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
-    raise |= tm[n] > s.top[n];
+    raise |= (tm[n] > s.top[n]) | (vtop * s.cs[n] > 512.0f);
   }
   if (__builtin_expect(__any(raise), 0)) {
-    // (cs is uniform: every column sees the same tokens' scales)
-    const float big = column_max(fminf(fmaxf(vtop, 0x1p-24f), 65504.0f));
-    const int e = (int)(__float_as_uint(big) >> 23);              // big < 2^(e - 126)
-    const float cs = __uint_as_float((uint32_t)(259 - e) << 23);  // big * cs < 2^6
-    float f = 1.0f;
-    if (big > s.limit) {
-      f = s.limit == 0.0f ? 1.0f : cs / s.cs;
-      s.cs = cs;
-      s.limit = 512.0f / cs;  // s_v * cs <= 2^9
-    }
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const float m = column_max(fmaxf(tm[n], s.m[n]));
@@ -412,13 +407,24 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
       s.m[n] = m;
       s.top[n] = m + 6.0f / s.mul[n];
       s.l[n] *= g;
-      s.rescale(n, f * g);
+      float big = s.big[n] * g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // (NaN does not count)
+        big = fmaxf(big, mul_zero(__builtin_amdgcn_exp2f(fmaf(x[n][i], s.mul[n], -m * s.mul[n])),
+                                  t.value_scale_again(i) * s.cs[n]));
+      big = column_max(fminf(big, 65504.0f * s.cs[n]));
+      // big < 2^(e - 126), and comes to [2^3, 2^4): weights down to 2^-17 of it keep
+      // fp16's full precision, and a value scale may be 32 times it before this
+      // branch is taken
+      const int e = (int)(__float_as_uint(big) >> 23), c = (int)(__float_as_uint(s.cs[n]) >> 23);
+      const int to = min(c + 130 - e, (int)(__float_as_uint(kMostCs) >> 23));
+      const float f = __uint_as_float((uint32_t)(127 + to - c) << 23);
+      s.cs[n] = __uint_as_float((uint32_t)to << 23);
+      s.big[n] = big * f;
+      s.rescale(n, g * f);
     }
   }
 
-  float svc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) svc[i] = t.value_scale(i) * s.cs;
   uint4 w[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
@@ -428,7 +434,7 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
     for (int i = 0; i < 8; ++i) {
       const float p = __builtin_amdgcn_exp2f(fmaf(x[n][i], s.mul[n], -mm));
       s.l[n] += p;
-      y[i] = mul_zero(p, svc[i]);  // an unseen token has no effect
+      y[i] = mul_zero(p, t.value_scale(i) * s.cs[n]);  // an unseen token has no effect
     }
     w[n] = make_uint4(pack2<kF16>(y[0], y[1]), pack2<kF16>(y[2], y[3]), pack2<kF16>(y[4], y[5]), pack2<kF16>(y[6], y[7]));
   }
@@ -626,7 +632,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_decode_kernel(Kv4AttnArgs 
     Reader<D, true>(a, sq, head, lane).walk(first, kStep, left, first + (left - 1) * kStep, [&](const Tile<D>& t, int t0) {
       if (!t.ok) return;
       FromRegisters<D> f(t, words[wave], lane, magic);
-      step<D, 1>(s, f, t0 + kKv4Tile > all_hi || t0 < all_lo, t0, q.len, ch);
+      step<D, 1>(s, f, t0 + kKv4Tile > all_hi || t0 < all_lo, t0, ch);
     });
 
     // join the waves: everything at the largest maximum, in true units
@@ -635,7 +641,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_decode_kernel(Kv4AttnArgs 
     __syncthreads();
     const float m = fmaxf(fmaxf(red_m[0][r], red_m[1][r]), fmaxf(red_m[2][r], red_m[3][r]));
     const float f = __builtin_amdgcn_exp2f(me - m);
-    const float fo = f / s.cs;
+    const float fo = f / s.cs[0];
     if (ch == 0) red_l[wave][r] = l * f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -760,8 +766,7 @@ struct StepLds {
   float top;
   int ok;
 
-  // (tokens past the end, `len`, get no value scale)
-  __device__ __forceinline__ void fill(const Tile<D>& t, int t0, int len, int lane, uint32_t magic) {
+  __device__ __forceinline__ void fill(const Tile<D>& t, int lane, uint32_t magic) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -771,7 +776,7 @@ struct StepLds {
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) v[x][lane] = o[x];
     const int i = lane & 31;
-    const uint32_t w = t0 + i < len ? finite_zero(t.sz) : 0u;
+    const uint32_t w = finite_zero(t.sz);
     const float sc = half_lo(w);
     if (lane < 32) {
       kw[i] = w;
@@ -810,11 +815,11 @@ struct FromLds {
       vs[4 * h] = c.x; vs[4 * h + 1] = c.y; vs[4 * h + 2] = c.z; vs[4 * h + 3] = c.w;
     }
   }
-  __device__ __forceinline__ void hide(int, int) {}
   __device__ __forceinline__ uint4 key(int h, int j) const { return t.k[h * (D / 32) + j][lane]; }
   __device__ __forceinline__ uint32_t key_word(int i) const { return kw[i]; }
   __device__ __forceinline__ float key_scale(int i) const { return ks[i]; }
   __device__ __forceinline__ float value_scale(int i) const { return vs[i]; }
+  __device__ __forceinline__ float value_scale_again(int i) const { return opaque(vs[i]); }
   __device__ __forceinline__ float largest() const { return t.top; }
   __device__ __forceinline__ uint4 zeros() const {
     const _Float16* const z = (lane & 3 ? t.rest : t.near) + 4 * ch;
@@ -901,7 +906,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_tile_kernel(Kv4AttnArgs a)
   const int last = max((q.len - 1) & ~(kKv4Tile - 1), 0);
   Reader<D, false>(a, sq, head, lane).walk(lo_w + kStep * s0 + kKv4Tile * wave, kStep, s1 - s0, last, [&](const Tile<D>& t, int t0) {
     lds_barrier();  // the steps before are done with
-    ops[wave].fill(t, t0, q.len, lane, magic);
+    ops[wave].fill(t, lane, magic);
     lds_barrier();
     const int base = t0 - kKv4Tile * wave;
 #pragma unroll 1
@@ -909,16 +914,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_tile_kernel(Kv4AttnArgs a)
       const int tu = base + kKv4Tile * u;
       if (tu >= hi || tu + kKv4Tile <= lo || !__builtin_amdgcn_readfirstlane(ops[u].ok)) continue;
       FromLds<D> f(ops[u], lane);
-      step<D, NC>(s, f, tu + kKv4Tile > all_hi || tu < all_lo, tu, q.len, ch);
+      step<D, NC>(s, f, tu + kKv4Tile > all_hi || tu < all_lo, tu, ch);
     }
   });
 
-  const float unit = 1.0f / s.cs;
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     const float l = column_sum(s.l[n]), me = s.m[n] * s.mul[n];
     if (row[n] < 0) continue;
-    const float z = s.zeros(n);
+    const float z = s.zeros(n), unit = 1.0f / s.cs[n];
     const float f = parts == 1 ? (l == 0.0f ? 0.0f : unit / l) : unit;  // no visible token: 0
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -137,3 +137,69 @@ def test_zero_points_are_exact_whole_numbers(D, max_q):
     half = 0.5 * np.spacing(np.abs(exact).astype(np.float16)).astype(np.float64)
     err = np.abs(got - exact)
     assert np.all(err <= half * (1 + 2.0 ** -8)), (err / half).max(axis=(1, 2))
+
+
+@pytest.mark.parametrize("hq,hk,D,dtype", [(8, 2, 128, torch.float16), (8, 1, 64, torch.bfloat16)])
+@pytest.mark.parametrize("size", [0.01, 0.001, 2.0 ** -20])
+def test_value_scales_of_unseen_tokens(hq, hk, D, dtype, size):
+    """The largest value scales, infinities and NaN, on tokens that no row sees
+    (below the window) and on tokens that only later rows see."""
+    lens, news = BATCH
+    cache, table, q = _batch(lens, news, hq, hk, D, 32, dtype, seed=23)
+    for i, n in enumerate(lens):
+        p, off = _held(cache, table[i], n)
+        cache["vsz"][p, :, off, 0] = (cache["vsz"][p, :, off, 0].astype(np.float32) * (size * 8)).astype(np.float16)
+    want = _expect(cache, table, lens, news, q, True, 21, D ** -0.5)
+    for odd in (65504, np.inf, np.nan):
+        bad = _copy(cache)
+        rows, at = [], 0
+        for i, (n, m) in enumerate(zip(lens, news)):
+            p, off = _held(cache, table[i], n)
+            hidden = np.arange(max(0, n - m - 20))
+            late = n - m + m // 2  # seen by the rows from m // 2 on
+            bad["vsz"][p[hidden], :, off[hidden], 0] = odd
+            bad["vsz"][p[late], :, off[late], 0] = odd
+            rows += range(at, at + m // 2)
+            at += m
+        for max_q in (1, 40):
+            print(f"hq={hq} D={D} size={size} odd={odd} max_q={max_q}", flush=True)
+            _close(_run(bad, table, lens, news, q, window=21, max_q=max_q), want, np.array(rows))
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+@pytest.mark.parametrize("place", [0, 40, 299])
+def test_a_large_value_scale_without_weight(place, max_q):
+    """A visible token of the largest value scale, whose score is so low that it
+    does not count, leaves the other tokens' weights as precise as without it."""
+    lens, news = [300, 300], [1, 20]
+    cache, table, q = _batch(lens, news, 8, 2, 128, 32, torch.float16, seed=24)
+    q = q.abs()
+    for i, n in enumerate(lens):
+        p, off = _held(cache, table[i], n)
+        cache["ksz"][p, :, off, 1] = -7
+        cache["vsz"][p, :, off, 0] = (cache["vsz"][p, :, off, 0].astype(np.float32) * 0.01).astype(np.float16)
+        cache["kq"][p[place], :, off[place]] = 0
+        cache["ksz"][p[place], :, off[place]] = 0.4, -20  # score about -90
+        cache["vsz"][p[place], :, off[place], 0] = 65504
+    want = _expect(cache, table, lens, news, q, True, 0, 128 ** -0.5)
+    _close(_run(cache, table, lens, news, q, max_q=max_q), want)
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+@pytest.mark.parametrize("rising", [True, False])
+def test_value_scales_against_scores(rising, max_q):
+    """Scores that rise along the context while value scales fall from the
+    largest to small ones (or the other way round): the weights that count are
+    small (or come first)."""
+    n = 400
+    lens, news = [n, n], [1, 20]
+    cache, table, q = _batch(lens, news, 8, 2, 128, 32, torch.float16, seed=25)
+    q = q.abs()
+    t = np.arange(n) if rising else np.arange(n)[::-1]
+    for i in range(2):
+        p, off = _held(cache, table[i], n)
+        cache["ksz"][p, :, off, 0] = 0.2
+        cache["ksz"][p, :, off, 1] = np.round(-22 + t / 20)[:, None]
+        cache["vsz"][p, :, off, 0] = (60000 * 2.0 ** (-t / 13.0))[:, None]
+    want = _expect(cache, table, lens, news, q, True, 0, 128 ** -0.5)
+    _close(_run(cache, table, lens, news, q, max_q=max_q), want)
