@@ -455,6 +455,13 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
 // A lane's accumulators: element i of accumulator x is its output channel
 // (D/4) c + (D/16) i + x.
 
+// The first token that a query at position pos sees.  (No difference that may
+// pass 31 bits: positions before the context's start are negative, windows go up to
+// 2^31 - 1.)
+__device__ __forceinline__ int first_seen(const Kv4AttnArgs& a, int pos) {
+  return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
 // A sequence's share of the work: its queries' columns in tiles of `width`
 // and the steps over the tokens that any of them sees.
 struct Seq {
@@ -467,7 +474,7 @@ __device__ __forceinline__ Seq seq_of(const Kv4AttnArgs& a, int s, int group, in
   q.q0 = a.cu_q ? min(max(a.cu_q[s], 0), (int)a.T) : s;
   q.n = a.cu_q ? min(max(a.cu_q[s + 1], q.q0), (int)a.T) - q.q0 : 1;
   const int first = q.len - q.n;  // position of the first query
-  q.lo = a.window > 0 ? max(first - a.window + 1, 0) & ~(kKv4Tile - 1) : 0;
+  q.lo = first_seen(a, first) & ~(kKv4Tile - 1);
   q.steps = max((q.len - q.lo + kStep - 1) / kStep, 1);  // at least one: every row is written
   q.tiles = (q.n * group + width - 1) / width;
   return q;
@@ -619,11 +626,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_decode_kernel(Kv4AttnArgs 
     s.clear();
     const int pos = q.len - q.n + qi;
     s.hi[0] = has ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
-    s.lo[0] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    s.lo[0] = first_seen(a, pos);
     // tokens that every column of the tile sees
     const int i0 = tile * 16 / group, i1 = min((tile * 16 + 15) / group, q.n - 1);
     const int all_hi = a.causal ? min(q.len - q.n + i0 + 1, q.len) : q.len;
-    const int all_lo = a.window > 0 ? max(q.len - q.n + i1 - a.window + 1, 0) : 0;
+    const int all_lo = first_seen(a, q.len - q.n + i1);
 
     // this wave's steps: tokens q.lo + 32 * (4 * (step0 + i) + wave)
     const int first = q.lo + kKv4Tile * (kWaves * step0 + wave);
@@ -882,12 +889,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv4_tile_kernel(Kv4AttnArgs a)
     load_queries<DT>(s, n, a.q + (q.q0 + qi) * a.ldq + (int64_t)hq[n] * D, has, ch, a.scale);
     const int pos = first + qi;
     s.hi[n] = has ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
-    s.lo[n] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    s.lo[n] = first_seen(a, pos);
   }
   s.clear();
   // tokens that some column of queries i0 .. i1 sees
   auto seen_to = [&](int i1) { return a.causal ? min(first + i1 + 1, q.len) : q.len; };
-  auto seen_from = [&](int i0) { return a.window > 0 ? max(first + i0 - a.window + 1, 0) : 0; };
+  auto seen_from = [&](int i0) { return first_seen(a, first + i0); };
   // of the wave: what some, and what every, column sees (no column: nothing)
   const bool any = c0 < q.n * group;
   const int i0 = c0 / group, i1 = min((c0 + 16 * NC - 1) / group, q.n - 1);

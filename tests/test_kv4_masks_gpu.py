@@ -74,7 +74,7 @@ def _close(got, want, rows=slice(None)):
     assert np.all(err <= tol[rows]), f"o: worst err/tol {np.nanmax(err / tol[rows]):.3f}, nan {np.isnan(err).sum()}"
     empty = np.isinf(rl[rows])
     assert np.array_equal(lse[rows][empty], rl[rows][empty])
-    assert np.all(np.abs(lse[rows] - rl[rows])[~empty] <= ltol[rows][~empty])
+    assert np.all(np.abs(lse[rows][~empty] - rl[rows][~empty]) <= ltol[rows][~empty])
 
 
 def _copy(cache):
@@ -203,3 +203,16 @@ def test_value_scales_against_scores(rising, max_q):
         cache["vsz"][p, :, off, 0] = (60000 * 2.0 ** (-t / 13.0))[:, None]
     want = _expect(cache, table, lens, news, q, True, 0, 128 ** -0.5)
     _close(_run(cache, table, lens, news, q, max_q=max_q), want)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 30])
+def test_windows_as_large_as_an_int(window):
+    """A window past every context hides nothing, also where a sequence has more
+    queries than tokens."""
+    lens, news = [3, 70, 0, 200, 1], [7, 3, 2, 40, 65]
+    for D in (64, 128):
+        cache, table, q = _batch(lens, news, 8, 4, D, 32, torch.float16, seed=26)
+        want = _expect(cache, table, lens, news, q, True, 0, D ** -0.5)
+        for max_q in (1, 65):
+            print(f"window={window} D={D} max_q={max_q}", flush=True)
+            _close(_run(cache, table, lens, news, q, window=window, max_q=max_q), want)
