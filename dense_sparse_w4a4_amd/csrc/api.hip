@@ -1081,8 +1081,11 @@ mq_status mq_kv4_attention(const uint16_t* q, int64_t ldq, int32_t dtype, int64_
              (long long)T, (long long)n_seqs);
   const int64_t qw = (int64_t)q_heads * head_dim;
   MQ_REQUIRE(ldq >= qw && ldo >= qw, MQ_ERR_SHAPE, "a leading dimension is below q_heads * head_dim");
-  MQ_REQUIRE(max_pages >= 0 && ld_table >= max_pages && max_pages < ((int64_t)1 << 31) / page_size, MQ_ERR_SHAPE,
-             "max_pages = %lld must be in [0, ld_table], with max_pages * page_size below 2^31", (long long)max_pages);
+  // (2^16: the kernels look a few steps past a sequence's end in 32 bits)
+  MQ_REQUIRE(max_pages >= 0 && ld_table >= max_pages &&
+                 max_pages <= (((int64_t)1 << 31) - ((int64_t)1 << 16)) / page_size,
+             MQ_ERR_SHAPE, "max_pages = %lld must be in [0, ld_table], with max_pages * page_size at most 2^31 - 2^16",
+             (long long)max_pages);
   MQ_REQUIRE(window >= 0, MQ_ERR_ARG, "window = %d must be >= 0", window);
   MQ_REQUIRE(scale == scale && scale > -__builtin_inff() && scale < __builtin_inff(), MQ_ERR_ARG,
              "scale must be finite");

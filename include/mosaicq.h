@@ -571,7 +571,8 @@ mq_status mq_kv4_append(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  * (NaN and infinities included) has no effect.
  *   q        : fp16 or bf16 (dtype) [T][ldq], heads side by side, D apart
  *   block_table : int32 [n_seqs][ld_table], max_pages of a row used; the
- *              tokens of a page index outside [0, n_pages) count as unseen
+ *              tokens of a page index outside [0, n_pages) count as unseen;
+ *              max_pages * page_size is at most 2^31 - 2^16
  *   kv_len   : int32 [n_seqs], clipped to [0, max_pages * page_size]
  *   cu_q     : int32 [n_seqs + 1], non-decreasing, clipped to [0, T]; NULL:
  *              one query per sequence (T == n_seqs).  Rows of q outside every

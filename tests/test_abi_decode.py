@@ -128,6 +128,20 @@ def test_kv4_attention_validation(L):
     assert call(T=0, ns=0, q=None, out=None, bt=None, kl=None) == OK
 
 
+def test_kv4_attention_token_counts_leave_room_in_32_bits(L):
+    """Positions are 32-bit, and steps are looked at past a sequence's end: the
+    most tokens of a table stop 2^16 short of 2^31 (window = -1, checked later,
+    stands for a call that is refused for nothing else)."""
+    def call(pages, page):
+        return L.mq_kv4_attention(P, 1024, 0, 3, 8, 2, 128, P, P, P, P, 5, page, P, 1 << 40, pages, 3, P, None, 1, 1, -1,
+                                  0.1, P, 1024, None, P, 1 << 30, None)
+    most = (1 << 31) - (1 << 16)
+    for page in (32, 64, 4096, 65536):
+        assert call(most // page, page) == ARG
+        assert call(most // page + 1, page) == SHAPE and call((1 << 31) // page - 1, page) == (
+            SHAPE if page < 65536 else ARG)
+
+
 @pytest.mark.skipif(not (os.path.exists(HIPCC) and shutil.which("g++")), reason="needs hipcc and g++")
 def test_decode_calls_under_host_sanitizers(tmp_path):
     """The host code of these calls with extreme sizes under AddressSanitizer
