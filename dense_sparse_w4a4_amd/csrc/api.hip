@@ -1000,6 +1000,9 @@ mq_status mq_kv4_append(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
              "rot_dim = %d must be a multiple of 16 in [0, head_dim]", rot_dim);
   MQ_REQUIRE(rot_dim == 0 || (n_positions > 0 && n_positions < ((int64_t)1 << 31)), MQ_ERR_SHAPE,
              "n_positions = %lld outside [1, 2^31)", (long long)n_positions);
+  // (a launch holds 2^32 threads, one for 16 channels)
+  MQ_REQUIRE(T * (q_heads + 2 * (int64_t)kv_heads) * head_dim <= ((int64_t)1 << 36) - 4096, MQ_ERR_SHAPE,
+             "T = %lld tokens: T * heads * head_dim must be at most 2^36 - 4096", (long long)T);
   MQ_REQUIRE(eps >= 0.0f && eps < __builtin_inff(), MQ_ERR_ARG, "eps must be finite and >= 0");
   if (T == 0) return MQ_OK;
   MQ_REQUIRE(q && k && v && slots && kq && ksz && vq && vsz && q_out, MQ_ERR_NULL_PTR,
@@ -1050,6 +1053,9 @@ static mq_status kv4_attn_shape(int64_t T, int64_t n_seqs, int32_t q_heads, int3
   MQ_REQUIRE(n_seqs >= 0 && n_seqs < ((int64_t)1 << 24), MQ_ERR_SHAPE, "n_seqs = %lld outside [0, 2^24)",
              (long long)n_seqs);
   MQ_REQUIRE(max_q >= 1, MQ_ERR_SHAPE, "max_q = %lld must be >= 1", (long long)max_q);
+  MQ_REQUIRE(kv4_attn_groups(T, n_seqs, q_heads, kv_heads, max_q) < (int64_t)1 << 24, MQ_ERR_SHAPE,
+             "T = %lld, n_seqs = %lld: T * q_heads / 128 + min(T, n_seqs) * kv_heads must be below 2^24 for prompts",
+             (long long)T, (long long)n_seqs);
   return MQ_OK;
 }
 

@@ -139,6 +139,8 @@ struct Kv4AttnArgs {
   float* lse;  // [T][q_heads] or null
   float* part;
 };
+// Workgroups of a launch: at most 2^24 - 1, 2^32 threads.
+int64_t kv4_attn_groups(int64_t T, int64_t seqs, int q_heads, int kv_heads, int64_t max_q);
 size_t kv4_attn_workspace(int64_t T, int64_t seqs, int q_heads, int kv_heads, int dim, int64_t max_q);
 hipError_t launch_kv4_attn(const Kv4AttnArgs& a, int64_t max_q, hipStream_t st);
 

@@ -997,7 +997,8 @@ constexpr int kTileNC = 2;
 bool takes_tiles(int64_t max_q, int group) { return max_q * group > 64; }
 int64_t tile_blocks(int64_t T, int64_t seqs, int group) {
   const int64_t width = kWaves * 16 * kTileNC;
-  return (T * group + width - 1) / width + seqs;  // every sequence may end in a part of a block
+  // every sequence that has queries may end in a part of a block
+  return (T * group + width - 1) / width + std::min(T, seqs);
 }
 // Token splits: enough workgroups for two per compute unit (its registers hold
 // no more), at most 16 (each costs the join a read of all outputs).
@@ -1008,6 +1009,11 @@ int tile_splits(int64_t T, int group, int kv_heads) {
 }
 
 }  // namespace
+
+int64_t kv4_attn_groups(int64_t T, int64_t seqs, int q_heads, int kv_heads, int64_t max_q) {
+  const int group = q_heads / kv_heads;
+  return takes_tiles(max_q, group) ? tile_blocks(T, seqs, group) * kv_heads : kDecodeGroups;
+}
 
 size_t kv4_attn_workspace(int64_t T, int64_t, int q_heads, int kv_heads, int dim, int64_t max_q) {
   const int group = q_heads / kv_heads;

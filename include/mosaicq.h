@@ -547,7 +547,8 @@ mq_status mq_w4a16_linear(const uint16_t* x, int32_t dtype, int64_t M, int64_t K
  *   q_weight, k_weight : x's type [D], or both NULL: no norm
  *   q_out    : x's type [T][ldqo]; may be q itself when ldqo == ldq
  *   k_out, v_out : x's type [T][kv_heads][D], or NULL
- *   leading dimensions are multiples of 8; T * (q_heads + 2*kv_heads) < 2^31.
+ *   leading dimensions are multiples of 8; T * (q_heads + 2*kv_heads) < 2^31,
+ *   and times D at most 2^36 - 4096
  */
 mq_status mq_kv4_append(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                         int32_t dtype, int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
@@ -578,7 +579,9 @@ mq_status mq_kv4_append(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  *              one query per sequence (T == n_seqs).  Rows of q outside every
  *              sequence are left as they are in out and lse.
  *   max_q    : the most queries of a sequence, which chooses the kernel: any
- *              value >= 1 gives the right result
+ *              value >= 1 gives the right result.  Above 64 query rows for a
+ *              key/value head (max_q * q_heads / kv_heads) a call takes
+ *              T * q_heads / 128 + min(T, n_seqs) * kv_heads below 2^24
  *   out      : q's type [T][ldo];  lse : fp32 [T][q_heads], or NULL
  *   workspace: device buffer of at least mq_kv4_attention_workspace's bytes
  *              (host output; 0 when T == 0 or n_seqs == 0), whatever its

@@ -142,6 +142,30 @@ def test_kv4_attention_token_counts_leave_room_in_32_bits(L):
             SHAPE if page < 65536 else ARG)
 
 
+def test_calls_larger_than_a_launch_are_refused(L):
+    """More threads than a launch holds (2^32): refused, not cut short.  ARG: a
+    later check, for a call that is refused for nothing else."""
+    def append(T, hq, hk, D):
+        return L.mq_kv4_append(P, 1 << 40, P, 1 << 40, P, 1 << 40, 0, T, hq, hk, D, P, None, None, 0, 0, 0, None, None,
+                               -1.0, P, P, P, P, 5, 32, P, 1 << 40, None, None, None)
+    assert append((1 << 26) - 4, 6, 1, 128) == ARG and append((1 << 26) - 3, 6, 1, 128) == SHAPE
+    assert append((1 << 27) - 8, 6, 1, 64) == ARG and append((1 << 27) - 7, 6, 1, 64) == SHAPE
+
+    n = ctypes.c_size_t(0)
+
+    def attend(T, seqs, hq, hk, max_q):
+        w = L.mq_kv4_attention_workspace(T, seqs, hq, hk, 128, max_q, ctypes.byref(n))
+        c = L.mq_kv4_attention(P, 1 << 40, 0, T, hq, hk, 128, P, P, P, P, 5, 32, P, 8, 8, seqs, P, P, max_q, 1, -1, 0.1,
+                               P, 1 << 40, None, P, 1 << 62, None)
+        assert (w == OK) == (c == ARG) and w in (OK, SHAPE) and c in (ARG, SHAPE)
+        return w
+    # many sequences, few of them with queries: only those take workgroups
+    assert attend(4, (1 << 24) - 1, 4096, 4096, 128) == OK
+    assert attend(1 << 20, 1 << 20, 8, 8, 128) == OK
+    assert attend(1 << 21, 1 << 21, 8, 8, 128) == SHAPE
+    assert attend(1 << 21, 1 << 21, 8, 8, 1) == OK  # the decoding kernel's grid is fixed
+
+
 @pytest.mark.skipif(not (os.path.exists(HIPCC) and shutil.which("g++")), reason="needs hipcc and g++")
 def test_decode_calls_under_host_sanitizers(tmp_path):
     """The host code of these calls with extreme sizes under AddressSanitizer
