@@ -88,6 +88,16 @@ __device__ __forceinline__ T opaque(T v) {
   return v;
 }
 
+// Between one lane's LDS stores and other lanes' loads of them in the same wave,
+// and before the next stores there: the LDS takes a wave's accesses in order, this
+// keeps the compiler from changing it (the words are stored one by one and loaded
+// four at a time, types that it may take for distinct memory).  No instruction.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float half_lo(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)w); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16)); }
 
@@ -325,9 +335,11 @@ struct FromRegisters {
       : t(tile), r(lane & 15), ch(lane >> 4), magic(m) {
     const uint32_t word = finite_zero(t.sz);
     const ZeroPair z = zero_pair(word);
+    wave_exchange();  // the step before has been read
     words[lane] = lane < 32 ? word : with_zero(word, z.near);
     words[lane ^ 96] = with_zero(word, z.rest);  // 64 .. 95; the keys' lanes' are not used
     const uint32_t* const values = words + (r & 3 ? 64 : 32);
+    wave_exchange();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 x = *reinterpret_cast<const uint4*>(words + 16 * h + 4 * ch);
