@@ -11,12 +11,17 @@
 //   fp16: 1024 + u (or 1024 + 16u one nibble higher), from which one packed
 //         operation on two codes takes 1032 (or a sixteenth, then 72): q
 //         exactly, 10 instructions per 8 codes
-//   bf16, which has no packed arithmetic: 128 + u; the surplus of 136 times
-//         the token's sum of x over the group enters as the accumulator's
-//         start, one chain of products of x with the constant -136 per group,
-//         shared by all channels of the workgroup
-// The group's scale is applied to the fp32 group sum, never rounded into a
-// weight.
+//   bf16, which has no packed arithmetic: (128 + u) 2^-15; the surplus of 136
+//         2^-15 times the token's sum of x over the group enters as the
+//         accumulator's start, one chain of products of x with the constant
+//         -136 2^-15 per group, shared by all channels of the workgroup.  The
+//         terms are up to 18 times the codes' own, and so is the rounding of
+//         their fp32 sums (some 2^-17 of sum |x| times the largest code in a
+//         group, against the output's 2^-9).  2^-15 keeps the sums of any finite
+//         x finite: 128 inputs times 143 2^-15 at most.  Small x loses nothing by
+//         it: the matrix core keeps subnormal products
+// The group's scale (for bf16, times 2^15) is applied to the fp32 group sum, never
+// rounded into a weight.
 //
 // Mapping: as the streaming kernel of the 4-bit route (slab layout: a group
 // of 16 channels is 1 KB contiguous and lane (r, c) holds channel r's 32
@@ -58,7 +63,7 @@ __device__ __forceinline__ v4f mfma_x(const uint4& a, const uint4& b, v4f c) {
 }
 
 // Eight two's-complement codes of a word, in the order 0, 4, 1, 5, 2, 6, 3, 7:
-// fp16 q, or bf16 136 + q.
+// fp16 q, or bf16 (136 + q) 2^-15.
 template <int DT>
 __device__ __forceinline__ uint4 code_operand(uint32_t w, uint32_t magic) {
   constexpr uint32_t m = 0x000F000Fu;
@@ -76,9 +81,9 @@ __device__ __forceinline__ uint4 order_x(const v4u& x) {
   return make_uint4(__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
                     __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u));
 }
-// bf16: the constant that takes the codes' surplus of 136 back out.
+// bf16: the constant -136 2^-15 that takes the codes' surplus back out.
 __device__ __forceinline__ uint4 surplus_operand() {
-  constexpr uint32_t c = 0xC308C308u;
+  constexpr uint32_t c = 0xBB88BB88u;
   return make_uint4(c, c, c, c);
 }
 
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(64 * KS) void w4a16_kernel(W4a16Args a) {
   const uint16_t* xp[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) xp[t] = row_of(16 * t + r);
-  const uint32_t magic = kv4_magic(DT == kF16 ? 0x64006400u : 0x43004300u);
+  const uint32_t magic = kv4_magic(DT == kF16 ? 0x64006400u : 0x3B803B80u);
 
   v4f y[MT][NS];
 #pragma unroll
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(64 * KS) void w4a16_kernel(W4a16Args a) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[t] = mfma_x<DT>(xo[t][j], c, acc[t]);
       }
-      const float sc = scale(s);
+      const float sc = DT == kBf16 ? scale(s) * 0x1p15f : scale(s);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
