@@ -598,6 +598,19 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return _FLOAT[t.dtype]
 
 
+def _workspace(t: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    """The caller's workspace where it is large enough, else one of the call's own
+    (None when none is needed)."""
+    if not nbytes:
+        return None
+    if t is not None:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        if t.numel() * t.element_size() >= nbytes:
+            return t
+    return like.new_empty(nbytes, dtype=torch.uint8)
+
+
 @functools.lru_cache(maxsize=1024)
 def w4a16_linear_workspace(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t(0)
@@ -618,6 +631,8 @@ def w4a16_linear(x: torch.Tensor, layer: PackedLayer, out: Optional[torch.Tensor
     N, b, ns = layer.N, layer.block, layer.col_idx.shape[0]
     if K != layer.K:
         raise ValueError("x must match the layer's K")
+    if not (layer.qw.is_cuda and layer.sw.is_cuda):
+        raise ValueError("the layer must hold device tensors")
     if out is None:
         out = x.new_empty((M, N))
     else:
@@ -625,14 +640,13 @@ def w4a16_linear(x: torch.Tensor, layer: PackedLayer, out: Optional[torch.Tensor
         if out.shape != (M, N) or out.stride(1) != 1:
             raise ValueError("out must be [M, N] with unit column stride")
     wsb = w4a16_linear_workspace(M, N, K)
-    if wsb and (workspace is None or workspace.numel() * workspace.element_size() < wsb):
-        workspace = x.new_empty(wsb, dtype=torch.uint8)
+    workspace = _workspace(workspace, wsb, x)
     _check("mq_w4a16_linear", lib().mq_w4a16_linear(
         x.data_ptr(), dt, M, K, x.stride(0) if M > 1 else K, N, layer.qw.data_ptr(),
         layer.sw.data_ptr(), b, ns, _ptr(layer.row_ptr) if ns else None,
         _ptr(layer.col_idx) if ns else None, _ptr(layer.qr) if ns else None,
         _ptr(layer.sr) if ns else None, out.data_ptr(), out.stride(0) if M > 1 else N,
-        _ptr(workspace) if wsb else None, wsb, _stream(stream)))
+        _ptr(workspace), wsb, _stream(stream)))
     return out
 
 
@@ -801,15 +815,14 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, k
     if max_q is None:
         max_q = 1 if cu_q is None else max(T, 1)
     wsb = kv4_attention_workspace(T, n, hq, cache.kv_heads, D, max_q)
-    if wsb and (workspace is None or workspace.numel() * workspace.element_size() < wsb):
-        workspace = q.new_empty(wsb, dtype=torch.uint8)
+    workspace = _workspace(workspace, wsb, q)
     _check("mq_kv4_attention", lib().mq_kv4_attention(
         q.data_ptr(), ldq, dt, T, hq, cache.kv_heads, D, cache.kq.data_ptr(), cache.ksz.data_ptr(),
         cache.vq.data_ptr(), cache.vsz.data_ptr(), cache.n_pages, cache.page_size, block_table.data_ptr(),
         block_table.stride(0) if n > 1 else pages, pages, n,
         _index(kv_len, torch.int32, n, "kv_len"),
         None if cu_q is None else _index(cu_q, torch.int32, n + 1, "cu_q"), max_q, int(causal), window,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(lse), _ptr(workspace) if wsb else None,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(lse), _ptr(workspace),
         wsb, _stream(stream)))
     return out
 

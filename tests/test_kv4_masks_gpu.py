@@ -216,3 +216,18 @@ def test_windows_as_large_as_an_int(window):
         for max_q in (1, 65):
             print(f"window={window} D={D} max_q={max_q}", flush=True)
             _close(_run(cache, table, lens, news, q, window=window, max_q=max_q), want)
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_host_and_overlapping_workspaces_are_refused(max_q):
+    cache = ops.kv4_cache(4, 32, 2, 64)
+    q = torch.zeros((3, 4, 64), dtype=torch.float16, device="cuda")
+    args = (q, cache, torch.zeros((3, 2), dtype=torch.int32, device="cuda"),
+            torch.ones(3, dtype=torch.int32, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda"), max_q)
+    need = ops.kv4_attention_workspace(3, 3, 4, 2, 64, max_q)
+    assert need > 0
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for bad in (torch.empty(need, dtype=torch.uint8), one.expand(need)):
+        with pytest.raises(ValueError, match="workspace"):
+            ops.kv4_attention(*args, workspace=bad)
+    assert not ops.kv4_attention(*args, workspace=one).any()

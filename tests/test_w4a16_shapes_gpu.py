@@ -48,3 +48,26 @@ def test_bf16_activations_near_the_smallest_and_largest(M, size):
     y = ops.w4a16_linear(x.cuda(), layer)
     _check(y, x, packed, torch.bfloat16)
     _check_rms(y, oracle.w4a16_reference(x.double().numpy(), packed), torch.bfloat16)
+
+
+def test_host_layers_and_workspaces_are_refused():
+    layer, _ = _layer(512, 512, 64, 0.1)
+    host = ops.PackedLayer(layer.N, layer.K, layer.block, layer.qw.cpu(), layer.sw.cpu(), layer.row_ptr, layer.col_idx,
+                           layer.qr, layer.sr)
+    x = _x(4, 512, torch.float16).cuda()
+    with pytest.raises(ValueError, match="device tensors"):
+        ops.w4a16_linear(x, host)
+    # (a layer of zeros whose inputs are split over workgroups, so that one is needed)
+    N, K, M = 4096, 8192, 16
+    need = ops.w4a16_linear_workspace(M, N, K)
+    assert need > 0
+    zeros = ops.PackedLayer(N, K, 64, torch.zeros((N // 16, K // 128, 64, 16), dtype=torch.uint8, device="cuda"),
+                            torch.zeros((N, K // 128), dtype=torch.float16, device="cuda"),
+                            *(layer.row_ptr[:0], layer.col_idx[:0], layer.qr[:0], layer.sr[:0]))
+    x = _x(M, K, torch.float16).cuda()
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for bad in (torch.empty(need, dtype=torch.uint8), one.expand(need), torch.zeros(2 * need, dtype=torch.uint8,
+                                                                                     device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            ops.w4a16_linear(x, zeros, workspace=bad)
+    assert not ops.w4a16_linear(x, zeros, workspace=one).any()  # too small: one of its own
