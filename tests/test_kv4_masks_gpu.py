@@ -231,3 +231,31 @@ def test_host_and_overlapping_workspaces_are_refused(max_q):
         with pytest.raises(ValueError, match="workspace"):
             ops.kv4_attention(*args, workspace=bad)
     assert not ops.kv4_attention(*args, workspace=one).any()
+
+
+@pytest.mark.parametrize("scale", [-3.0, 3.0])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 50])
+def test_sharp_softmax_under_windows(D, scale, window):
+    """Outputs and log-sums where nearly all weight is on one token."""
+    lens, news = [300, 70, 3, 0], [9, 40, 1, 1]
+    cache, table, q = _batch(lens, news, 8, 2, D, 32, torch.float16, seed=27)
+    want = _expect(cache, table, lens, news, q, True, window, scale)
+    for max_q in (1, 40):
+        _close(_run(cache, table, lens, news, q, window=window, scale=scale, max_q=max_q), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_precision_of_scores(D, dtype, max_q):
+    """One visible token: the log-sum is its score.  Root mean square error over
+    that of the scores: the key codes' products lose two bits, 1.1e-7 (the error was
+    1.8e-6 where they lost six); the chain of sums of codes, about twice the score
+    before the zero point's share is added, 1.1e-7; the queries' sum, scale and units
+    0.7e-7: 1.7e-7 in all, held to 2^-21."""
+    n = 512
+    cache, table, q = _batch([1] * n, [1] * n, 8, 2, D, 32, dtype, seed=28)
+    _, lse, _, _ = _expect(cache, table, [1] * n, [1] * n, q, True, 0, D ** -0.5)
+    _, got = _run(cache, table, [1] * n, [1] * n, q, max_q=max_q)
+    assert np.sqrt(np.mean((got - lse) ** 2)) <= 2.0 ** -21 * np.sqrt(np.mean(lse ** 2))
