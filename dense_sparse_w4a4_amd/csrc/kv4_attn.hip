@@ -349,7 +349,7 @@ struct FromRegisters {
     }
   }
   __device__ __forceinline__ uint4 key(int h, int j) const { return codes8(t.k[h][j]); }
-  __device__ __forceinline__ uint32_t key_word(int i) const { return kw[i]; }
+  __device__ __forceinline__ float key_zero(int i) const { return half_hi(kw[i]); }
   __device__ __forceinline__ float key_scale(int i) const { return half_lo(kw[i]); }
   __device__ __forceinline__ float value_scale(int i) const { return half_lo(vw[i]); }
   __device__ __forceinline__ float value_scale_again(int i) const { return half_lo(opaque(vw[i])); }
@@ -389,7 +389,7 @@ __device__ __forceinline__ void step(Columns<D, NC>& s, F& t, bool edge, int t0,
   for (int i = 0; i < 8; ++i) {
     const float sk = t.key_scale(i);
 #pragma unroll
-    for (int n = 0; n < NC; ++n) x[n][i] = fmaf(half_hi(t.key_word(i)), s.qsum[n], a[n][i >> 2][i & 3]) * sk;
+    for (int n = 0; n < NC; ++n) x[n][i] = fmaf(t.key_zero(i), s.qsum[n], a[n][i >> 2][i & 3]) * sk;
   }
   if (__builtin_expect(edge, 0)) {
 #pragma unroll
@@ -779,8 +779,7 @@ __global__ __launch_bounds__(64 * W) void kv4_join_kernel(Kv4AttnArgs a) {
 template <int D>
 struct StepLds {
   uint4 k[D / 16][64], v[D / 16][64];  // [operand][lane]
-  uint32_t kw[32];
-  float ks[32], vs[32];
+  float kz[32], ks[32], vs[32];  // (widened once here: the fused operation on a half costs two of the fp32 one's)
   _Float16 near[32], rest[32];  // of zero point + 8
   float top;
   int ok;
@@ -798,7 +797,7 @@ struct StepLds {
     const uint32_t w = finite_zero(t.sz);
     const float sc = half_lo(w);
     if (lane < 32) {
-      kw[i] = w;
+      kz[i] = half_hi(w);
       ks[i] = sc;
     } else {
       vs[i] = sc;
@@ -820,22 +819,21 @@ template <int D>
 struct FromLds {
   const StepLds<D>& t;
   int lane, ch;
-  uint32_t kw[8];
-  float ks[8], vs[8];
+  float kz[8], ks[8], vs[8];
 
   __device__ __forceinline__ FromLds(const StepLds<D>& s, int l) : t(s), lane(l), ch(l >> 4) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 a = *reinterpret_cast<const uint4*>(t.kw + 16 * h + 4 * ch);
+      const float4 a = *reinterpret_cast<const float4*>(t.kz + 16 * h + 4 * ch);
       const float4 b = *reinterpret_cast<const float4*>(t.ks + 16 * h + 4 * ch);
       const float4 c = *reinterpret_cast<const float4*>(t.vs + 16 * h + 4 * ch);
-      kw[4 * h] = a.x; kw[4 * h + 1] = a.y; kw[4 * h + 2] = a.z; kw[4 * h + 3] = a.w;
+      kz[4 * h] = a.x; kz[4 * h + 1] = a.y; kz[4 * h + 2] = a.z; kz[4 * h + 3] = a.w;
       ks[4 * h] = b.x; ks[4 * h + 1] = b.y; ks[4 * h + 2] = b.z; ks[4 * h + 3] = b.w;
       vs[4 * h] = c.x; vs[4 * h + 1] = c.y; vs[4 * h + 2] = c.z; vs[4 * h + 3] = c.w;
     }
   }
   __device__ __forceinline__ uint4 key(int h, int j) const { return t.k[h * (D / 32) + j][lane]; }
-  __device__ __forceinline__ uint32_t key_word(int i) const { return kw[i]; }
+  __device__ __forceinline__ float key_zero(int i) const { return kz[i]; }
   __device__ __forceinline__ float key_scale(int i) const { return ks[i]; }
   __device__ __forceinline__ float value_scale(int i) const { return vs[i]; }
   __device__ __forceinline__ float value_scale_again(int i) const { return opaque(vs[i]); }
