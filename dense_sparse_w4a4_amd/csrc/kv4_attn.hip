@@ -142,7 +142,9 @@ __device__ __forceinline__ uint32_t with_zero(uint32_t word, _Float16 z) {
   return (word & 0xFFFFu) | ((uint32_t)__builtin_bit_cast(uint16_t, z) << 16);
 }
 
-// ONCE: the words are read by this wave alone and pass the caches by.
+// ONCE: the words pass the caches by.  One wave reads them, with up to 16 query
+// columns per key/value head in a sequence; above, every tile of 16 columns reads
+// them again (64 sequences of 2048 tokens: 16 columns 35 us, 32 62, 64 109).
 template <bool ONCE, typename T>
 __device__ __forceinline__ T load_words(const uint8_t* p) {
   if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
@@ -576,8 +578,8 @@ struct Shared {
 // Bound by the cache's bytes once contexts are long, by the launches and the
 // latency of one pass of dependent loads when short (64 query heads on 8, 128
 // channels, with the join): 131075 and 92684 tokens, 244 MB: 54 us, 4.5 TB/s;
-// 64 ragged sequences of 512 to 8192 tokens, 199 MB: 58 us, 3.4 TB/s; one
-// sequence of 1000 tokens (32 heads): 10.6 us.  The work is cut into equal runs
+// 64 ragged sequences of 512 to 8192 tokens, 199 MB: 58-60 us, 3.4 TB/s; one
+// sequence of 1000 tokens (32 heads): 10.8 us.  The work is cut into equal runs
 // of steps rather than by sequence or head, so that ragged batches and few long
 // contexts fill the card alike.  Eight waves per workgroup, or 384, 768 or 1024
 // workgroups instead of 512, gained nothing.
@@ -860,11 +862,14 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // Bound by the vector instructions of the softmax beside the matrix products:
 // per 32 x 32 scores of a wave 34 matrix instructions of 16 cycles, and for a
 // lane's 16 scores scale, zero point, maximum, exponential (16 cycles), sum,
-// weight and conversion, some 800 cycles.  1024 queries over 8192 tokens (64
-// heads on 8, 128 channels, 258 GFLOP): 380 us, 680 TFLOP/s; with every wave
-// unpacking for itself 1061 us.  Moving the next step's scores ahead of this
-// one's exponentials (380 -> 409 us) lost and reading operands ahead gained
-// nothing: two waves per SIMD already overlap the units.
+// weight and conversion, some 800 cycles; and, third, by the operands' way from
+// LDS.  1024 queries over 8192 tokens (64 heads on 8, 128 channels, 258 GFLOP): 342
+// us in a row of calls, 750 TFLOP/s (384 us as the profiler times it); with every
+// wave unpacking for itself 1061 us.  Counters of that run: vector unit issuing 63%
+// of the time, matrix core busy 33%, LDS reads some 60%, so no unit is full and
+// they overlap in part: between the barriers unpacking comes before use.  Moving
+// the next step's scores ahead of this one's exponentials lost 7%, reading
+// operands ahead gained nothing.
 template <int DT, int D, int NC>
 __global__ __launch_bounds__(64 * kWaves, 2) void kv4_tile_kernel(Kv4AttnArgs a) {
   constexpr int WIDTH = kWaves * 16 * NC;
@@ -1003,7 +1008,9 @@ constexpr int kTileNC = 2;
 // above them the tile kernel.  Times in us, decoding / tile kernel, 64 heads on
 // 8:  64 sequences of 2048 tokens, 16 columns 35 / 139, 32: 62 / 126, 64: 109 /
 // 136, 128: 179 / 162;  8 of 512, 64 columns 16 / 36, 128: 23 / 40;  one of
-// 8192, 32 columns 29 / 27, 64: 31 / 29, 128: 33 / 33.
+// 8192, 32 columns 29 / 27, 64: 31 / 29, 128: 33 / 33.  So on short contexts the
+// decoding kernel would win above 64 columns, too; the rule looks at the columns
+// alone.
 bool takes_tiles(int64_t max_q, int group) { return max_q * group > 64; }
 int64_t tile_blocks(int64_t T, int64_t seqs, int group) {
   const int64_t width = kWaves * 16 * kTileNC;

@@ -32,13 +32,15 @@
 // once per group, shared by the slabs.
 //
 // Bound by the weights' bytes for few tokens (N K/2, read once per 16 MT
-// tokens), by unpacking beside the matrix products for many.  A tenth of the
-// blocks as residual: 1 token 4096->4096 5.7 us (9.6 MB, 1.7 TB/s: a launch and
-// one round of loads); 4 tokens 4096->14336 11.8 us (33.6 MB, 2.8 TB/s); 16
-// tokens 5120->25600 (bf16) 20.6 us (75 MB, 3.7 TB/s); 50 tokens 25600->5120 44
-// us (78 MB and 14.4 GFLOP: 1.8 TB/s, 330 TFLOP/s); these with two layers in
-// turn, the weights partly in the last-level cache; with six in turn, from
-// memory, in a graph: 6.7, 12.3, 27.5 (fp16) and 49.6 us.
+// tokens).  For many no unit is full: a wave has few groups, so that the start,
+// the residual and the join weigh as much as its stream, and four token tiles with
+// four slabs spill some registers.  A tenth of the blocks as residual: 1 token
+// 4096->4096 5.9 us (9.6 MB, 1.6 TB/s: a launch and one round of loads); 4 tokens
+// 4096->14336 12.2 us (33.6 MB, 2.7 TB/s); 16 tokens 5120->25600 (bf16) 21 us (75
+// MB, 3.6 TB/s); 50 tokens 25600->5120 45 us (78 MB and 14.4 GFLOP: 1.7 TB/s, 320
+// TFLOP/s; vector unit issuing 37% of the time, matrix core busy 21%); these with
+// two layers in turn, the weights partly in the last-level cache; with six in
+// turn, from memory, in a graph: 6.7, 12.3, 27.5 (fp16) and 49.6 us.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

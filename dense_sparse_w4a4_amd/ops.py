@@ -790,8 +790,9 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, k
     fp16 or bf16; block_table int32 [n_seqs, max_pages]; kv_len int32 [n_seqs]
     tokens held, the queries' own among them; cu_q int32 [n_seqs + 1] first
     query row of each sequence (None: one query each).  max_q, the most queries
-    of a sequence (default: all of T when cu_q is given), only chooses the
-    kernel.  scale defaults to D ** -0.5.  lse fp32 [T, q_heads] receives the
+    of a sequence, only chooses the kernel, but give it with cu_q: left out, it is
+    all of T, and a batch of few queries each takes the kernel for prompts (64
+    sequences of 2048 tokens, one query each: 139 us instead of 35).  scale defaults to D ** -0.5.  lse fp32 [T, q_heads] receives the
     log of each row's softmax sum.  A row that sees no token gets 0 (lse -inf).
     Returns out [T, q_heads, D]."""
     dt = _float_type(q, "q")

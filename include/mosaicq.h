@@ -499,9 +499,10 @@ mq_status mq_validate_csr(const int32_t* row_ptr, const int32_t* col_idx,
  *              (host output; often 0), whatever its contents; the call owns it
  *              until the stream has drained
  * Any M is right; the kernel is made for decoding batches (it reads the
- * weights once per 64 tokens).  A token with a non-finite activation gets
- * non-finite y.  Sums run in a fixed order: repeated calls give identical
- * bits.
+ * weights once per 16, 32 or 64 tokens, by the layer's size and M).  A token with
+ * a non-finite activation gets non-finite y; the sums over a group's finite
+ * activations are finite, however large those are.  Sums run in a fixed order:
+ * repeated calls give identical bits.
  */
 mq_status mq_w4a16_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes);
 mq_status mq_w4a16_linear(const uint16_t* x, int32_t dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,
@@ -513,7 +514,8 @@ mq_status mq_w4a16_linear(const uint16_t* x, int32_t dtype, int64_t M, int64_t K
  * The 4-bit cache.  n_pages pages of page_size tokens (a power of two, 32 to
  * 65536) of every key/value head; head_dim D is 64 or 128.  Per token and
  * head, keys and values are D codes u in 0..15, a scale s (fp16, >= 0) and a
- * zero point z (fp16, a whole number); the value held is s * (u + z).
+ * zero point z (fp16, a whole number); the value held is s * (u + z).  A z that is
+ * not finite makes the value NaN, whatever s and u.
  *   kq  : uint8 [n_pages][kv_heads][page_size][D/2]; code d of a token is in
  *         byte d/2, the low nibble first
  *   vq  : uint8 [n_pages][kv_heads][page_size/4][D/8][4][4]; code d of token t
@@ -586,9 +588,12 @@ mq_status mq_kv4_append(const uint16_t* q, int64_t ldq, const uint16_t* k, int64
  *   workspace: device buffer of at least mq_kv4_attention_workspace's bytes
  *              (host output; 0 when T == 0 or n_seqs == 0), whatever its
  *              contents; the call owns it until the stream has drained
- * Scores, sums and outputs accumulate in fp32; the weights p are rounded to
- * fp16 for their product with the values.  Parts of a long context are joined
- * in a fixed order: repeated calls give identical bits.
+ * Scores, sums and outputs accumulate in fp32; queries are rounded to fp16 (after
+ * a power of two of the row's own: fp16 and bf16 hold their digits), the products
+ * of queries and key codes lose their two lowest bits, and the weights p * s are
+ * rounded to fp16 (after a power of two that keeps those that count in its normal
+ * range) for their product with the values.  Parts of a long context are joined in
+ * a fixed order: repeated calls give identical bits.
  */
 mq_status mq_kv4_attention_workspace(int64_t T, int64_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                      int64_t max_q, size_t* bytes);
